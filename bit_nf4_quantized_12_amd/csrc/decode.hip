@@ -208,29 +208,39 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
 }
 
 // o of one head from its parts: lane i of every wave holds part i's weight
-// (at most 64 parts), wave w adds the parts w, w + 4, ..., the four sums are
-// added in order.
+// (at most 64 parts). Wave w adds the parts 8 t + 2 w in its lower half and
+// 8 t + 2 w + 1 in its upper half, t = 0, 1, ...; lane l & 31 of a half holds 4
+// columns. The halves, then the waves, are added in order. Every lane runs every
+// step, with columns or without: a lane that is switched off gives no weight.
+// Steps past the last part repeat it with weight 0 (and the value 0, so that
+// no infinity is multiplied by it).
 __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a) {
   __shared__ f32x4 f[4][kMaxD / 4];
   const int64_t bh = blockIdx.x;
-  const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
   const float* st = a.stat + bh * 2 * a.nsplit;
   const bool in = l < a.nsplit;
   const float mi = in ? st[2 * l] : -__builtin_inff(), si = in ? st[2 * l + 1] : 0.f;
   const float m = wave_max(mi);
   const float g = mi == -__builtin_inff() ? (si == 0.f ? 0.f : 1.f) : fast_exp2((mi - m) * a.scale * kAttnLog2e);
   const float sum = wave_sum(g * si);
-  const int cols = a.D / 4;  // at most 32: half a wave takes every second part
+  const int cols = a.D / 4;  // at most 32
   const int half = l >> 5, col = l & 31;
+  const float* p = a.part + bh * a.nsplit * a.D + 4 * min(col, cols - 1);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  if (col < cols) {
-    const float* p = a.part + bh * a.nsplit * a.D + 4 * col;
-#pragma unroll 4
-    for (int i = 2 * w + half; i < a.nsplit; i += 8) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(p + (int64_t)i * a.D);
-      const float gi = __shfl(g, i);
+  constexpr int U = 4;  // parts of a lane on their way together
+  for (int i0 = 2 * w; i0 < a.nsplit; i0 += 8 * U) {  // (the same steps in all lanes of a wave)
+    f32x4 v[U];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(gi, v[r], acc[r]);
+    for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(i0 + half + 8 * u, a.nsplit - 1) * a.D);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + half + 8 * u;
+      const bool ok = i < a.nsplit;
+      const float from = __shfl(g, i & 63);  // (outside of the choice)
+      const float gi = ok ? from : 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(gi, ok ? v[u][r] : 0.f, acc[r]);
     }
   }
 #pragma unroll
