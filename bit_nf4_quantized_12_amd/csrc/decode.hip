@@ -47,7 +47,8 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
   const int total = first + n - lo;    // visible keys
   int chunk = (total + a.nsplit - 1) / a.nsplit;
   chunk = (chunk + 4 * kStep - 1) / (4 * kStep) * (4 * kStep);
-  const int beg = min(total, split * chunk), end = min(total, beg + chunk);
+  // (of nearly 2^31 positions, the last part's own end would pass 2^31)
+  const int beg = min(total, split * chunk), end = beg + min(total - beg, chunk);
 
   const uint16_t* kp = a.k + b * a.k_sb + hk * a.k_sh;
   const uint16_t* vp = a.v + b * a.v_sb + hk * a.v_sh;

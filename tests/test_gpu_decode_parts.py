@@ -51,3 +51,17 @@ def test_filled_parts(d, parts):
 def test_parts_that_a_short_request_leaves_empty(d):
     _check([40000, 39999, 39, 8704], 40000, 2, 1, d)
     _check([16384, 700], 16384, 16, 2, d)
+
+
+def test_a_cache_of_nearly_2_31_positions():
+    """The last of 64 parts ends past 2^31 - 128. Keys that are all one row (token pitch 0) give every position the same
+    probability, 1 / cap; all sums are whole numbers below 2^24 or counts of 32 keys, so only the quotient rounds."""
+    cap, ones = (1 << 31) - 4097, 1 << 24
+    report(f"decode: cap={cap} D=8")
+    vc = torch.zeros(1, cap, 1, 8, dtype=torch.bfloat16, device=DEV)
+    vc[:, cap - ones:] = 1
+    kc = torch.ones(1, 1, 1, 8, dtype=torch.bfloat16, device=DEV).expand(1, cap, 1, 8)
+    lens = torch.tensor([cap], dtype=torch.int32, device=DEV)
+    o = q.qlora_window_attn_decode(torch.ones(1, 1, 8, dtype=torch.bfloat16, device=DEV), kc, vc, lens, 1 << 40, 0)
+    ref = np.full(8, ones / cap)
+    wa._within(o[0, 0], ref, (wa.H + 16 * wa.U) * ref, "o")
