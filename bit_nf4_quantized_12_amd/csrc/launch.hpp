@@ -21,6 +21,10 @@ inline hipError_t ensure_lds(const void* fn, int bytes, std::atomic<uint32_t>& d
   return e;
 }
 
+// Workgroups that one launch takes along x. A grid of 2^32 threads or more is
+// not refused: its workgroups past that count do not run, without an error.
+inline int64_t launch_limit(int64_t threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 struct GemmParams {
   const uint16_t* act;     // [M, Kred] bf16, row pitch Kred
   const uint8_t* codes;    // NF4 codes of W [wN, wK]

@@ -331,11 +331,15 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
 
 template <typename T, typename P, int VEC, int TPR, int NV>
 void run_fwd(const NormArgs& a, hipStream_t s) {
-  constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
-  hipLaunchKernelGGL((norm_fwd_kernel<T, P, VEC, TPR, NV>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)),
-                     dim3(TPR < 256 ? 256 : TPR), 0, s, static_cast<const T*>(a.x), a.ldx,
-                     static_cast<const P*>(a.w), static_cast<const P*>(a.b), a.M, (int)a.C, 1.0f / (float)a.C, a.eps,
-                     static_cast<T*>(a.y), a.mean, a.rstd);
+  constexpr int ROWS = TPR < 256 ? 256 / TPR : 1, THREADS = TPR < 256 ? 256 : TPR;
+  const int64_t most = launch_limit(THREADS) * ROWS;  // 2^24 rows of 520 columns (17 GB of bf16) are more
+  for (int64_t r = 0; r < a.M; r += most) {
+    const int64_t n = a.M - r < most ? a.M - r : most;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, P, VEC, TPR, NV>), dim3((unsigned)((n + ROWS - 1) / ROWS)), dim3(THREADS), 0,
+                       s, static_cast<const T*>(a.x) + r * a.ldx, a.ldx, static_cast<const P*>(a.w),
+                       static_cast<const P*>(a.b), n, (int)a.C, 1.0f / (float)a.C, a.eps,
+                       static_cast<T*>(a.y) + r * a.C, a.mean + r, a.rstd + r);
+  }
 }
 
 template <typename T, typename P, int VEC, int TPR, int NV>
