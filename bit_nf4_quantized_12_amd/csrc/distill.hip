@@ -428,6 +428,22 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(DistillArgs a, int par
   if (g != 0.f) store_entries<T>(dzr, en, a.K, c, Z, 0.f, base, shift, P, g, keep0, keep1);
 }
 
+// Rows r .. r + n - 1 of a call: what one launch takes of more rows.
+DistillArgs rows_of(const DistillArgs& a, int64_t r, int64_t n) {
+  DistillArgs b = a;
+  b.M = n;
+  auto from = [](const void* p, int64_t elements, int size) { return static_cast<const char*>(p) + elements * size; };
+  b.z = from(a.z, r * a.ldz, a.z_f32 ? 4 : 2);
+  b.val = from(a.val, r * a.K, a.val_f32 ? 4 : 2);
+  b.idx = from(a.idx, r * a.K, a.idx_64 ? 8 : 4);
+  if (a.t_lse) b.t_lse = a.t_lse + r;
+  if (a.weight) b.weight = a.weight + r;
+  if (a.loss) b.loss = a.loss + r;
+  b.lse = a.lse + r;
+  if (a.dz) b.dz = static_cast<char*>(a.dz) + r * a.lddz * (a.z_f32 ? 4 : 2);
+  return b;
+}
+
 template <typename T, bool GRAD>
 hipError_t run_row(const DistillArgs& a, hipStream_t s) {
   constexpr int N = Chunk<T>::N;
@@ -437,14 +453,19 @@ hipError_t run_row(const DistillArgs& a, hipStream_t s) {
   // and 15.5 us with 4 and 16 chunks at 128 rows, 21.7 and 22.5 at 512, 39 and 36 at
   // 1024, 134 and 120 at 4096).
   auto threads = [&](int64_t nv) { return ((chunks + nv - 1) / nv + 63) / 64 * 64; };
-  const dim3 grid((unsigned)a.M);
   const int64_t nv = a.M >= 1024 ? 16 : 4;
-  if (threads(4) <= 1024 && (nv == 4 || threads(16) < 128))
-    hipLaunchKernelGGL((distill_row_kernel<T, 4, GRAD>), grid, dim3((unsigned)threads(4)), 0, s, a);
-  else if (threads(16) <= 1024)
-    hipLaunchKernelGGL((distill_row_kernel<T, 16, GRAD>), grid, dim3((unsigned)threads(16)), 0, s, a);
-  else
-    hipLaunchKernelGGL((distill_row_kernel<T, 0, GRAD>), grid, dim3(1024), 0, s, a);
+  const bool few = threads(4) <= 1024 && (nv == 4 || threads(16) < 128), held = threads(16) <= 1024;
+  const int64_t nt = few ? threads(4) : held ? threads(16) : 1024, most = launch_limit(nt);
+  for (int64_t r = 0; r < a.M; r += most) {
+    const DistillArgs b = rows_of(a, r, a.M - r < most ? a.M - r : most);
+    const dim3 grid((unsigned)b.M), block((unsigned)nt);
+    if (few)
+      hipLaunchKernelGGL((distill_row_kernel<T, 4, GRAD>), grid, block, 0, s, b);
+    else if (held)
+      hipLaunchKernelGGL((distill_row_kernel<T, 16, GRAD>), grid, block, 0, s, b);
+    else
+      hipLaunchKernelGGL((distill_row_kernel<T, 0, GRAD>), grid, block, 0, s, b);
+  }
   return hipGetLastError();
 }
 
@@ -459,11 +480,15 @@ hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t s) {
   const int64_t n = a.z_f32 ? 4 : 8;
   const int64_t chunks = (a.V + n - 1) / n + 1;
   const int parts = (int)((chunks + kBwdChunks - 1) / kBwdChunks);
-  const dim3 grid((unsigned)(a.M * parts));
-  if (a.z_f32)
-    hipLaunchKernelGGL(distill_bwd_kernel<float>, grid, dim3(256), 0, s, a, parts);
-  else
-    hipLaunchKernelGGL(distill_bwd_kernel<uint16_t>, grid, dim3(256), 0, s, a, parts);
+  const int64_t most = launch_limit(256) / parts;
+  for (int64_t r = 0; r < a.M; r += most) {
+    const DistillArgs b = rows_of(a, r, a.M - r < most ? a.M - r : most);
+    const dim3 grid((unsigned)(b.M * parts));
+    if (a.z_f32)
+      hipLaunchKernelGGL(distill_bwd_kernel<float>, grid, dim3(256), 0, s, b, parts);
+    else
+      hipLaunchKernelGGL(distill_bwd_kernel<uint16_t>, grid, dim3(256), 0, s, b, parts);
+  }
   return hipGetLastError();
 }
 

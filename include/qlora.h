@@ -498,10 +498,10 @@ typedef struct {
   float temperature;    /* > 0 */
 } qlora_topk_distill;
 
-/* loss, lse: float32 [M]. Errors: NULL, SHAPE (M < 1, M or M V / 16384 too
- * large for one launch, V < 1, K out of range, ldz < V), ALIGN (z, val, idx 16
- * bytes; the float32 arrays 4), UNSUPPORTED (a dtype; temperature not finite
- * or not positive), DEVICE. */
+/* loss, lse: float32 [M]. Errors: NULL, SHAPE (M < 1, M (V / 16384 + 1) of
+ * 2^31 or more, V < 1, V >= 2^31 - 64, K out of range, ldz < V), ALIGN (z,
+ * val, idx 16 bytes; the float32 arrays 4), UNSUPPORTED (a dtype; temperature
+ * not finite or not positive), DEVICE. */
 int qlora_topk_distill_fwd(const qlora_topk_distill* d, float* loss, float* lse, void* stream);
 
 /* dz [M, V] of z_dtype, row pitch lddz >= V, from the lse of the forward and

@@ -34,3 +34,23 @@ def test_layer_norm_rows():
     got = q.qlora_layer_norm_fwd(_repeat(x, times), w, b)
     for a, t in zip(got, want):
         assert _repeats(a, t)
+
+
+def test_distillation_rows():
+    times, V, K = 16400, 16, 2  # loss: 64 threads per row, gradient: 256
+    report(f"distill: M={times * BASE} V={V} K={K}")
+    assert times * BASE > 1 << 26
+    g = torch.Generator().manual_seed(2)
+    z, val = torch.randn(BASE, V, generator=g).bfloat16().to(DEV), torch.randn(BASE, K, generator=g).to(DEV)
+    idx = torch.randint(-1, V, (BASE, K), generator=g).int().to(DEV)
+    t_lse, weight = torch.rand(BASE, generator=g).to(DEV) + 2, torch.rand(BASE, generator=g).to(DEV)
+    small = (z, val, idx, t_lse, weight)
+    big = [_repeat(t, times) for t in small]
+    want = q.qlora_topk_distill_fwd_bwd(*small[:3], weight, 2.0, t_lse)
+    got = q.qlora_topk_distill_fwd_bwd(*big[:3], big[4], 2.0, big[3])
+    for a, t in zip(got, want):
+        assert _repeats(a, t)
+    loss, lse = q.qlora_topk_distill_fwd(*big[:3], 2.0, big[3])
+    assert torch.equal(loss, got[0]) and torch.equal(lse, got[1])
+    dz = q.qlora_topk_distill_bwd(*big[:3], lse, big[4], 2.0, big[3])
+    assert _repeats(dz, q.qlora_topk_distill_bwd(*small[:3], want[1], weight, 2.0, t_lse))
