@@ -34,12 +34,15 @@ int check_norm(const void* x, int64_t ldx, int x_dtype, const void* w, int w_dty
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-int check_attn_sizes(const qlora_window_attn* a) {
+// threads: of the largest workgroup that takes a sequence's head (forward 256,
+// backward 512). A launch has room for one of them for each (fit_groups).
+constexpr int kFwdThreads = 256, kBwdThreads = 512;
+int check_attn_sizes(const qlora_window_attn* a, int threads) {
   if (a->B < 1 || a->B >= 65536 || a->Tq < 1 || a->Tq >= kInt32 || a->Tk < 1 || a->Tk >= kInt32) return QLORA_ERR_SHAPE;
   if (a->H < 1 || a->Hkv < 1 || a->H % a->Hkv != 0 || a->H >= 65536) return QLORA_ERR_SHAPE;
   if (a->max_q < 1 || a->max_q >= kInt32 - 256 || a->max_k < 1 || a->max_k >= kInt32 - 256) return QLORA_ERR_SHAPE;
   const int64_t blocks = a->B * ((std::max(a->max_q, a->max_k) + 127) / 128);
-  if (blocks * a->H >= kInt32 / 4) return QLORA_ERR_SHAPE;
+  if (blocks * a->H >= kInt32 / 4 || (a->B + 7) * a->H > launch_limit(threads) - 256) return QLORA_ERR_SHAPE;
   if (a->D < 8 || a->D > 128 || a->D % 8 != 0) return QLORA_ERR_UNSUPPORTED;
   if (a->window < 1 || a->sinks < 0 || a->sinks > kMaxSinks) return QLORA_ERR_UNSUPPORTED;
   if (!std::isfinite(a->scale) || !(a->scale > 0.0f)) return QLORA_ERR_UNSUPPORTED;
@@ -57,9 +60,9 @@ int view_heads(const qlora_heads* t, AttnTensor& v) {
   return QLORA_OK;
 }
 
-int fill_attn(const qlora_window_attn* a, AttnArgs& r) {
+int fill_attn(const qlora_window_attn* a, AttnArgs& r, int threads) {
   if (!a->cu_q || !a->cu_k) return QLORA_ERR_NULL;
-  const int st = check_attn_sizes(a);
+  const int st = check_attn_sizes(a, threads);
   if (st != QLORA_OK) return st;
   if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4)) return QLORA_ERR_ALIGN;
   r.cu_q = a->cu_q;
@@ -240,7 +243,7 @@ int qlora_window_attn_fwd(const qlora_window_attn* a, const qlora_heads* q, cons
                           const qlora_heads* v, const qlora_heads* o, float* lse, void* stream) {
   if (!a || !lse) return QLORA_ERR_NULL;
   AttnArgs r{};
-  int st = fill_attn(a, r);
+  int st = fill_attn(a, r, kFwdThreads);
   if (st == QLORA_OK) st = view_heads(q, r.q);
   if (st == QLORA_OK) st = view_heads(k, r.k);
   if (st == QLORA_OK) st = view_heads(v, r.v);
@@ -256,7 +259,7 @@ int qlora_window_attn_fwd(const qlora_window_attn* a, const qlora_heads* q, cons
 }
 
 size_t qlora_window_attn_bwd_workspace_bytes(const qlora_window_attn* a) {
-  return a && check_attn_sizes(a) == QLORA_OK ? plan_bwd(a).total : 0;
+  return a && check_attn_sizes(a, kBwdThreads) == QLORA_OK ? plan_bwd(a).total : 0;
 }
 
 int qlora_window_attn_bwd(const qlora_window_attn* a, const qlora_heads* q, const qlora_heads* k,
@@ -265,7 +268,7 @@ int qlora_window_attn_bwd(const qlora_window_attn* a, const qlora_heads* q, cons
                           size_t ws_bytes, void* stream) {
   if (!a || !lse) return QLORA_ERR_NULL;
   AttnArgs r{};
-  int st = fill_attn(a, r);
+  int st = fill_attn(a, r, kBwdThreads);
   if (st == QLORA_OK) st = view_heads(q, r.q);
   if (st == QLORA_OK) st = view_heads(k, r.k);
   if (st == QLORA_OK) st = view_heads(v, r.v);

@@ -220,8 +220,9 @@ hipError_t run_fwd(const AttnArgs& a, hipStream_t s) {
   hipError_t e = ensure_lds(reinterpret_cast<const void*>(attn_fwd_kernel<DP, NW, NS>), bytes, done);
   if (e != hipSuccess) return e;
   const int64_t blocks = (a.max_q + 32 * NW - 1) / (32 * NW);
-  const int nq = block_groups(blocks, blocks * a.B * a.H, 2);
-  const UnitGrid ug((int64_t)a.B * a.Hkv, (int64_t)nq * (a.H / a.Hkv));
+  const int64_t units = (int64_t)a.B * a.Hkv, group = a.H / a.Hkv;
+  const int nq = fit_groups(block_groups(blocks, blocks * a.B * a.H, 2), units, group, 64 * NW);
+  const UnitGrid ug(units, nq * group);
   hipLaunchKernelGGL((attn_fwd_kernel<DP, NW, NS>), ug.grid(), dim3(64 * NW), bytes, s, a, nq, ug);
   return hipGetLastError();
 }

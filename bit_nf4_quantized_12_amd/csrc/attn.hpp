@@ -234,6 +234,14 @@ inline int block_groups(int64_t blocks, int64_t all, int64_t most) {
   m = m < 1 ? 1 : m > most ? most : m;
   return (int)((blocks + m - 1) / m);
 }
+// `groups` such groups of a head, or as many as a launch takes of `per` heads
+// (or parts) for each of `units` units: a UnitGrid of n per items has at most
+// (units + 7) n per + 256 workgroups, its own rounding included. What a group
+// does not come to in one turn it does in the next, so fewer cost time only.
+inline int fit_groups(int64_t groups, int64_t units, int64_t per, int threads) {
+  const int64_t most = (launch_limit(threads) - 256) / ((units + 7) * per);
+  return (int)(groups < most ? groups : most < 1 ? 1 : most);
+}
 struct UnitItem {
   int unit, item;
 };

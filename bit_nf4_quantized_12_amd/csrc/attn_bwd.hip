@@ -565,8 +565,9 @@ hipError_t run_dkv(const AttnArgs& a, const float* joined, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int64_t longest = a.max_k < a.Tk ? a.max_k : a.Tk;
   const int64_t units = (int64_t)a.B * a.Hkv, blocks = (longest + kKeys - 1) / kKeys;
-  const int nk = block_groups(blocks, blocks * units, 4);
-  const UnitGrid ug(units, (int64_t)nk * (CUT ? a.parts : 1));
+  const int64_t parts = CUT ? a.parts : 1;
+  const int nk = fit_groups(block_groups(blocks, blocks * units, 4), units, parts, 64 * kKeyWaves * NS);
+  const UnitGrid ug(units, nk * parts);
   hipLaunchKernelGGL((attn_dkv_kernel<DP, NS, CUT>), ug.grid(), dim3(64 * kKeyWaves * NS), bytes, s, a, nk, joined, ug);
   const hipError_t le = hipGetLastError();
   if (le != hipSuccess || !CUT) return le;
@@ -585,7 +586,7 @@ hipError_t run_bwd(const AttnArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   const int64_t units = (int64_t)a.B * a.Hkv, group = a.H / a.Hkv;
   const int64_t bq = (a.max_q + kRows - 1) / kRows;
-  const int nq = block_groups(bq, bq * units * group, 2);
+  const int nq = fit_groups(block_groups(bq, bq * units * group, 2), units, group, 256);
   const UnitGrid uq(units, nq * group);
   hipLaunchKernelGGL((attn_dq_kernel<DP>), uq.grid(), dim3(256), dq_bytes, s, a, nq, uq);
   e = hipGetLastError();
@@ -598,7 +599,7 @@ hipError_t run_bwd(const AttnArgs& a, hipStream_t s) {
   // 575).
   if (a.sinks > 0 && (int64_t)a.max_k > 2 * ((int64_t)kKeys + a.window) + 1024) {
     const int span = attn_sink_span(a.max_q);
-    const int nr = (a.max_q + span - 1) / span;
+    const int nr = fit_groups((a.max_q + span - 1) / span, units, group, 64 * kSinkWaves);
     float* share = a.sink;
     joined = share + attn_sink_slots(a.Tq, a.B, a.max_q) * a.H * (2 * kMaxSinks * DP);
     const UnitGrid ur(units, nr * group);

@@ -433,8 +433,9 @@ typedef struct {
 /* o = softmax(scale q k^T) v over the visible keys; o [Tq, H, D] bf16, lse
  * float32 [H, Tq] = log sum exp of the scaled scores. Rows of no sequence are
  * not written. Errors: NULL, SHAPE (sizes out of range, H % Hkv, B H
- * ceil(longest / 128) of 2^29 or more), ALIGN (p: 16 bytes; pitches; lse, cu_q, cu_k: 4 bytes),
- * UNSUPPORTED (D, window, sinks or scale out of range), DEVICE. */
+ * ceil(longest / 128) of 2^29 or more, (B + 7) H of 2^24 - 256 or more; in the
+ * backward 2^23 - 256), ALIGN (p: 16 bytes; pitches; lse, cu_q, cu_k: 4
+ * bytes), UNSUPPORTED (D, window, sinks or scale out of range), DEVICE. */
 int qlora_window_attn_fwd(const qlora_window_attn* a, const qlora_heads* q, const qlora_heads* k,
                           const qlora_heads* v, const qlora_heads* o, float* lse, void* stream);
 
