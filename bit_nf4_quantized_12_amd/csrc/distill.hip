@@ -181,13 +181,16 @@ template <typename T>
 __device__ __forceinline__ void load_logit(Entry& e, const T* zr, int64_t keep0, int64_t keep1) {
   if (e.i >= keep0 && e.i < keep1) e.z = Chunk<T>::one(zr[e.i]);
 }
+// Puts the entry into LDS and returns its value for the row's maximum. A maximum
+// skips NaN: infinity stands in for it, so that a row of NaN is not taken for
+// one without entries and its sums of (t - maximum) become NaN.
 __device__ __forceinline__ float keep_entry(const DistillArgs& a, const Entry& e, int k, Entries& en) {
   if (k < (a.K + 3) / 4 * 4) {  // whole groups of 4 are compared
     en.idx[k] = (int)e.i;
     en.t[k] = e.t;
     en.z[k] = e.z;
   }
-  return e.t;
+  return e.t == e.t ? e.t : __builtin_inff();
 }
 // The entries past the first of each thread; returns the largest value.
 template <typename T>
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(1024) void distill_row_kernel(DistillArgs a) {
   const float lsum = log2_hw(sum);
   const float Z = zmax + lsum * (kLn2 * a.tau);  // tau lse
   if (!a.t_lse) shift = log2_hw(tsum);
-  const float P = none ? 0.f : (a.t_lse ? tsum : 1.f);
+  const float P = none ? 0.f : (a.t_lse || tsum != tsum ? tsum : 1.f);
 
   if (tid < 64) {
     float part = 0.f;
@@ -398,7 +401,7 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(DistillArgs a, int par
     if (en.idx[k] >= 0 && en.t[k] != -__builtin_inff()) tsum += exp2_hw((en.t[k] - base) * c - shift);
   block_reduce<SumOf>(tsum, zero, red[1]);
   if (!a.t_lse) shift = log2_hw(tsum);
-  const float P = none ? 0.f : (a.t_lse ? tsum : 1.f);
+  const float P = none ? 0.f : (a.t_lse || tsum != tsum ? tsum : 1.f);
   const float Z = a.lse[row] * a.tau;
   const float g = none ? 0.f : (a.weight ? a.weight[row] : 1.f) * a.tau;
   const float gp = g * P;

@@ -62,7 +62,7 @@ def topk_distill(z, val, idx, tau, t_lse=None, weight=None):
     for m in range(M):
         zz = z[m] / tau
         lse[m] = zz.max() + np.log(np.exp(zz - zz.max()).sum())
-        has = (idx[m] >= 0) & (idx[m] < V) & (val[m] > -np.inf)
+        has = (idx[m] >= 0) & (idx[m] < V) & ~np.isneginf(val[m])
         if not has.any():
             continue
         t, at = val[m][has] / tau, idx[m][has]
