@@ -8,8 +8,9 @@
 //   loss = tau^2 sum_k p_k (log p_k - z[i_k] / tau + lse)
 //   dz_j = weight tau (P q_j - sum over k with i_k = j of p_k)
 // (tau^2 keeps the gradient's size independent of the temperature.) A row
-// without entries, or of weight zero, gives a zero gradient whatever its
-// logits hold; entries of probability zero add nothing to the loss.
+// without an entry of positive probability, or of weight zero, gives a zero
+// gradient whatever its logits hold; entries of probability zero add nothing to
+// the loss.
 //
 // The one-pass kernel keeps the row in the registers of its workgroup, so a
 // step reads the logits once and writes the gradient once: the loss alone
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(1024) void distill_row_kernel(DistillArgs a) {
   if constexpr (!GRAD) return;
 
   const float w = a.weight ? a.weight[row] : 1.f;
-  const float g = none ? 0.f : w * a.tau;
+  const float g = P == 0.f ? 0.f : w * a.tau;
   const float gp = g * P;
   T* dzr = static_cast<T*>(a.dz) + row * a.lddz;
   const bool whole = misalign(dzr) == off;
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(256) void distill_bwd_kernel(DistillArgs a, int par
   if (!a.t_lse) shift = log2_hw(tsum);
   const float P = none ? 0.f : (a.t_lse || tsum != tsum ? tsum : 1.f);
   const float Z = a.lse[row] * a.tau;
-  const float g = none ? 0.f : (a.weight ? a.weight[row] : 1.f) * a.tau;
+  const float g = P == 0.f ? 0.f : (a.weight ? a.weight[row] : 1.f) * a.tau;
   const float gp = g * P;
   T* dzr = static_cast<T*>(a.dz) + row * a.lddz;
   const bool whole = misalign(dzr) == off;

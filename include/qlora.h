@@ -484,8 +484,8 @@ int qlora_window_attn_decode(const qlora_cache* q, const qlora_cache* k, const q
  *         tau);  P = sum p_k
  *   loss = tau^2 sum_k p_k (log p_k - log q[idx_k])
  *   dz_j = weight tau (P q_j - sum over idx_k = j of p_k)
- * A row without an entry of positive probability has loss 0 and gradient 0; a
- * row of weight 0 has gradient 0 whatever its logits hold. An entry whose value
+ * A row without an entry of positive probability has loss 0 and gradient 0, a
+ * row of weight 0 has gradient 0, whatever their logits hold. An entry whose value
  * is NaN makes its row's loss NaN, and its gradient where the weight is not 0. */
 typedef struct {
   int64_t M, V, K;      /* 1 <= K <= 1024 */

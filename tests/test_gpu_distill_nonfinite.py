@@ -38,3 +38,15 @@ def test_teacher_values_that_are_nan(K, mass, dt, V):
         assert torch.all(dz[[4, 5]] == 0) and loss[5] == 0
         for i in (0, 3, 6):
             assert torch.equal(loss[i], loss0[i]) and torch.equal(dz[i], dz0[i])
+
+
+@pytest.mark.parametrize("dt,V", [("f32", 300), ("bf16", 32000), ("bf16", 140001)])
+def test_entries_of_probability_zero_and_logits_that_are_no_numbers(dt, V):
+    report(f"distill, probabilities of zero: V={V} {dt}")
+    z, val, idx, t_lse, weight = td._make(6, V, 5, dt, 2.0, True, 3, ragged=False)
+    weight[:] = 1
+    t_lse[1:4] = 1e30  # exp(val / tau - t_lse) = 0
+    z[1, 7], z[2, 8], z[3, 9] = NAN, INF, -INF
+    for loss, dz in _both(z, val, idx, weight, t_lse):
+        assert torch.all(loss[1:4] == 0) and torch.all(dz[1:4] == 0)
+        assert torch.all(loss[[0, 4, 5]] != 0) and torch.isfinite(dz).all()
