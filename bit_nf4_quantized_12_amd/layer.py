@@ -200,14 +200,18 @@ def _heads(t, dev, name, shape=None):
 
 
 def _heads_out(t, shape, dev, name):
-    """A new [tokens, heads, D] tensor, or the caller's (a slice of a larger one, for instance) after
-    checking that its elements lie apart."""
+    """A new [tokens, heads, D] tensor, or the caller's (a slice of a larger one, or heads first, for instance)
+    after checking that its elements lie apart."""
     if t is None:
         t = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
     view = _heads(t, dev, name, shape)
-    if not (view.head_pitch >= shape[2] and view.token_pitch >= (shape[1] - 1) * view.head_pitch + shape[2]):
-        raise ValueError(f"{name} must not overlap itself")
+    # from the smaller pitch to the larger, each steps over all that lies below it (a pitch of one element is not used)
+    below = shape[2]
+    for pitch, n in sorted((p, n) for p, n in ((view.token_pitch, shape[0]), (view.head_pitch, shape[1])) if n > 1):
+        if pitch < below:
+            raise ValueError(f"{name} must not overlap itself")
+        below += (n - 1) * pitch
     return t, view
 
 
