@@ -6,12 +6,13 @@ Argument marshalling for the C ABI (include/qlora.h), with the conventions of
 the package: every tensor on one GPU, work on that GPU's current stream, outputs
 new tensors unless the caller hands in his own, ``QloraError`` for a status of
 the library. The ``...Function`` classes at the end wrap the calls for torch's
-automatic differentiation.
+automatic differentiation, once: the gradient of a gradient is refused.
 """
 
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import QLORA_BF16, QLORA_F32, _check, load_library, new_workspace
 
@@ -408,6 +409,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -425,6 +427,7 @@ class WindowAttnFunction(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse, cu = ctx.saved_tensors
         longest, window, sinks, scale = ctx.rest
@@ -444,6 +447,7 @@ class TopkDistillFunction(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         logits, t_val, t_idx, lse, t_lse = ctx.saved_tensors
         grad = qlora_topk_distill_bwd(logits, t_val, t_idx, lse, dloss.contiguous(), ctx.temperature, t_lse)

@@ -1,0 +1,46 @@
+"""The autograd functions of norm, attention and distillation inside larger
+graphs."""
+
+import pytest
+import torch
+
+import bit_nf4_quantized_12_amd as q
+from tests import test_gpu_distill as td
+from tests import test_gpu_window_attn as wa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _randn(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(shape, generator=g).to(dtype).to(DEV)
+
+
+def _attn(qt, kt, vt, cu, n, *rest):
+    return q.WindowAttnFunction.apply(qt, kt, vt, cu, n, 30, 2, None, *rest)
+
+
+def _norm_graph():
+    g = torch.Generator().manual_seed(1)
+    x, w, b = (_randn(g, *s, dtype=torch.float32).requires_grad_() for s in ((4, 32), (32,), (32,)))
+    return q.LayerNormFunction.apply(x, w, b, 1e-5), x
+
+
+def _attn_graph():
+    leaf = [t.requires_grad_() for t in wa._make([20], [20], 2, 2, 64, 1)[:3]]
+    return _attn(*leaf, wa._starts([20]), 20), leaf[0]
+
+
+def _distill_graph():
+    z, val, idx, _, _ = td._make(4, 50, 6, "f32", 2.0, False, 7)
+    z.requires_grad_()
+    return q.TopkDistillFunction.apply(z, val, idx, 2.0, None), z
+
+
+@pytest.mark.parametrize("graph", [_norm_graph, _attn_graph, _distill_graph])
+def test_derivatives_of_gradients_are_refused(graph):
+    out, leaf = graph()
+    grad, = torch.autograd.grad(out.float().square().sum(), leaf, create_graph=True)
+    # a penalty on the gradient beside another term: it must not be left out in silence
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (grad.float().square().sum() + leaf.float().sum()).backward()
