@@ -44,6 +44,7 @@ import threading
 from collections import namedtuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqlora.so")
@@ -489,6 +490,7 @@ class LoRALinear4bitFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, A, B, T = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.W, X, A, B, dY.contiguous(), T, ctx.scale,

@@ -1,5 +1,5 @@
-"""The autograd functions of norm, attention and distillation inside larger
-graphs."""
+"""The autograd functions of the linears, norm, attention and distillation inside
+larger graphs."""
 
 import pytest
 import torch
@@ -37,7 +37,14 @@ def _distill_graph():
     return q.TopkDistillFunction.apply(z, val, idx, 2.0, None), z
 
 
-@pytest.mark.parametrize("graph", [_norm_graph, _attn_graph, _distill_graph])
+def _linear_graph():
+    g = torch.Generator().manual_seed(1)
+    weight = q.quantize_weight(_randn(g, 64, 64))
+    x, a, b = (_randn(g, *s).requires_grad_() for s in ((8, 64), (8, 64), (64, 8)))
+    return q.LoRALinear4bitFunction.apply(x, a, b, weight, 2.0), x
+
+
+@pytest.mark.parametrize("graph", [_linear_graph, _norm_graph, _attn_graph, _distill_graph])
 def test_derivatives_of_gradients_are_refused(graph):
     out, leaf = graph()
     grad, = torch.autograd.grad(out.float().square().sum(), leaf, create_graph=True)
