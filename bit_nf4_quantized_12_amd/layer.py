@@ -417,22 +417,23 @@ class LayerNormFunction(torch.autograd.Function):
 
 
 class WindowAttnFunction(torch.autograd.Function):
-    """o of qlora_window_attn_fwd for q, k, v of sequences that start at cu [B + 1]."""
+    """o of qlora_window_attn_fwd for q, k, v of sequences that start at cu [B + 1]; after prefixes, keys and
+    values of sequences that start at cu_k (longest_k: the longest one's keys, None: all of k)."""
 
     @staticmethod
-    def forward(ctx, q, k, v, cu, longest, window, sinks, scale):
-        o, lse = qlora_window_attn_fwd(q, k, v, cu, longest, window, sinks, scale=scale)
-        ctx.save_for_backward(q, k, v, o, lse, cu)
-        ctx.rest = (longest, window, sinks, scale)
+    def forward(ctx, q, k, v, cu, longest, window, sinks, scale, cu_k=None, longest_k=None):
+        o, lse = qlora_window_attn_fwd(q, k, v, cu, longest, window, sinks, cu_k=cu_k, scale=scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu, cu_k)
+        ctx.rest = (longest, window, sinks)
+        ctx.opts = dict(max_k=longest_k, scale=scale)
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_o):
-        q, k, v, o, lse, cu = ctx.saved_tensors
-        longest, window, sinks, scale = ctx.rest
-        grads = qlora_window_attn_bwd(q, k, v, o, lse, d_o.contiguous(), cu, longest, window, sinks, scale=scale)
-        return (*grads, None, None, None, None, None)
+        q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
+        grads = qlora_window_attn_bwd(q, k, v, o, lse, d_o.contiguous(), cu, *ctx.rest, cu_k=cu_k, **ctx.opts)
+        return (*grads, None, None, None, None, None, None, None)
 
 
 class TopkDistillFunction(torch.autograd.Function):

@@ -51,3 +51,17 @@ def test_derivatives_of_gradients_are_refused(graph):
     # a penalty on the gradient beside another term: it must not be left out in silence
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (grad.float().square().sum() + leaf.float().sum()).backward()
+
+
+def test_attention_after_a_prefix():
+    lq, lk = [30, 1, 50], [90, 200, 50]
+    qt, kt, vt, gt = wa._make(lq, lk, 4, 2, 64, 6)
+    cu_q, cu_k = wa._starts(lq), wa._starts(lk)
+    leaf = [t.clone().requires_grad_() for t in (qt, kt, vt)]
+    o = _attn(*leaf, cu_q, 50, cu_k, 200)
+    o.backward(gt)
+    fwd = q.qlora_window_attn_fwd(qt, kt, vt, cu_q, 50, 30, 2, cu_k=cu_k)
+    assert torch.equal(o, fwd[0])
+    for t, x in zip(leaf, q.qlora_window_attn_bwd(qt, kt, vt, *fwd, gt, cu_q, 50, 30, 2, cu_k=cu_k, max_k=200)):
+        assert torch.equal(t.grad, x)
+    wa._oracle_check(qt, kt, vt, gt, lq, lk, 30, 2, 64 ** -0.5, fwd, [t.grad for t in leaf])
