@@ -398,12 +398,42 @@ def qlora_topk_distill_fwd_bwd(logits, t_val, t_idx, row_weight=None, temperatur
 # automatic differentiation
 # ---------------------------------------------------------------------------
 
+# Other operations leave slices that start off 16 bytes (rows of an odd width from the second on), expanded and
+# transposed tensors; the calls above refuse them, the functions below copy them.
+
+def _aligned(t):
+    """t as a contiguous tensor that starts on 16 bytes (itself, or a copy); None stays."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _rows(t):
+    """[M, C] t itself where the calls take it: contiguous rows that lie apart and start on 16 bytes; else a copy."""
+    if t.dim() != 2:
+        return t
+    ok = (t.shape[1] == 1 or t.stride(1) == 1) and (t.shape[0] == 1 or t.stride(0) >= t.shape[1])
+    return t if ok and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _head_rows(t):
+    """[tokens, heads, D] t itself where the calls take it (contiguous along D, pitches of 16-byte multiples within
+    their limits); else a copy."""
+    if t.dim() != 3:
+        return t
+    (T, H, D), (st, sh, sd) = t.shape, t.stride()
+    ok = ((D == 1 or sd == 1) and (T == 1 or (0 < st < 1 << 24 and st % 8 == 0))
+          and (H == 1 or (sh < 1 << 31 and sh % 8 == 0)))
+    return t if ok and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 class LayerNormFunction(torch.autograd.Function):
     """y = layer norm of x [M, C] with weight and bias (bias may be None)."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        x = x if x.stride(1) == 1 else x.contiguous()
+        x, weight, bias = _rows(x), _aligned(weight), _aligned(bias)
         y, mean, rstd = qlora_layer_norm_fwd(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         return y
@@ -413,7 +443,7 @@ class LayerNormFunction(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        return (*qlora_layer_norm_bwd(x, weight, dy.contiguous(), mean, rstd, *need[:3]), None)
+        return (*qlora_layer_norm_bwd(x, weight, _aligned(dy), mean, rstd, *need[:3]), None)
 
 
 class WindowAttnFunction(torch.autograd.Function):
@@ -422,6 +452,7 @@ class WindowAttnFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, cu, longest, window, sinks, scale, cu_k=None, longest_k=None):
+        q, k, v = _head_rows(q), _head_rows(k), _head_rows(v)
         o, lse = qlora_window_attn_fwd(q, k, v, cu, longest, window, sinks, cu_k=cu_k, scale=scale)
         ctx.save_for_backward(q, k, v, o, lse, cu, cu_k)
         ctx.rest = (longest, window, sinks)
@@ -432,7 +463,7 @@ class WindowAttnFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, d_o):
         q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
-        grads = qlora_window_attn_bwd(q, k, v, o, lse, d_o.contiguous(), cu, *ctx.rest, cu_k=cu_k, **ctx.opts)
+        grads = qlora_window_attn_bwd(q, k, v, o, lse, _aligned(d_o), cu, *ctx.rest, cu_k=cu_k, **ctx.opts)
         return (*grads, None, None, None, None, None, None, None)
 
 
@@ -441,7 +472,7 @@ class TopkDistillFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, t_val, t_idx, temperature, t_lse):
-        logits = logits if logits.stride(1) == 1 else logits.contiguous()
+        logits, t_val, t_idx = _rows(logits), _aligned(t_val), _aligned(t_idx)
         loss, lse = qlora_topk_distill_fwd(logits, t_val, t_idx, temperature, t_lse)
         ctx.save_for_backward(logits, t_val, t_idx, lse, t_lse)
         ctx.temperature = temperature
