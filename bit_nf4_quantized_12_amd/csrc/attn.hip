@@ -211,6 +211,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_fwd_kernel(AttnArgs a, int nq
 
     if (have) store_rows<DP>(a, st, sv, hq, iq, l);
   }
+  if (b == a.B - 1) {  // rows past the last sequence see nothing
+    const int64_t rest = sv.q0 + sv.Lq;
+    zero_rows(a.o, hq, rest, a.Tq, a.D, x, nq);
+    for (int64_t r = rest + x * blockDim.x + tid; r < a.Tq; r += nq * blockDim.x)
+      a.lse[(int64_t)hq * a.Tq + r] = -__builtin_inff();
+  }
 }
 
 template <int DP, int NW, int NS>

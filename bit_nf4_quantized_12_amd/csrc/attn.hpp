@@ -207,6 +207,15 @@ __device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int b) {
   return v;
 }
 
+// Rows first .. last - 1 of head h become zero: share x of n workgroups' work. (Of
+// rows that belong to no sequence: an array may be longer than its batch.)
+__device__ __forceinline__ void zero_rows(const AttnTensor& t, int h, int64_t first, int64_t last, int D, int x, int n) {
+  const int C = D / 8;  // 16-byte chunks of a row
+  for (int64_t e = (int64_t)x * blockDim.x + threadIdx.x; e < (last - first) * C; e += (int64_t)n * blockDim.x)
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.p) + (first + e / C) * t.st + h * t.sh + e % C * 8) =
+        make_uint4(0, 0, 0, 0);
+}
+
 // Workgroup g runs on XCD g % 8. A unit is a sequence's key head; its work is
 // `per` items (blocks of rows, times query heads), all of which read the same
 // keys and values, so a unit's items run one after another on one XCD and meet

@@ -180,6 +180,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int nq, Uni
         }
     }
   }
+  if (b == a.B - 1) zero_rows(a.dq, hq, sv.q0 + sv.Lq, a.Tq, a.D, x, nq);
 }
 
 // ---------------------------------------------------------------------------
@@ -444,6 +445,10 @@ __global__ __launch_bounds__(64 * kKeyWaves * NS, 2) void attn_dkv_kernel(AttnAr
       *reinterpret_cast<uint2*>(vd + col) = make_uint2(pack_bf16(av[0], av[1]), pack_bf16(av[2], av[3]));
     }
   }
+  if (!CUT && b == a.B - 1) {
+    zero_rows(a.dk, hk, sv.k0 + sv.Lk, a.Tk, a.D, x, nk);
+    zero_rows(a.dv, hk, sv.k0 + sv.Lk, a.Tk, a.D, x, nk);
+  }
 }
 
 // dk and dv from the parts' shares, in order. A workgroup takes 8 keys of a
@@ -466,6 +471,10 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs a) {
     const AttnTensor& t = which ? a.dv : a.dk;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + row * t.st + hk * t.sh + col) =
         make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+  }
+  if (b == a.B - 1) {
+    zero_rows(a.dk, hk, sv.k0 + sv.Lk, a.Tk, a.D, blockIdx.x, gridDim.x);
+    zero_rows(a.dv, hk, sv.k0 + sv.Lk, a.Tk, a.D, blockIdx.x, gridDim.x);
   }
 }
 

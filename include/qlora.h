@@ -431,8 +431,9 @@ typedef struct {
 } qlora_window_attn;
 
 /* o = softmax(scale q k^T) v over the visible keys; o [Tq, H, D] bf16, lse
- * float32 [H, Tq] = log sum exp of the scaled scores. Rows of no sequence are
- * not written. Errors: NULL, SHAPE (sizes out of range, H % Hkv, B H
+ * float32 [H, Tq] = log sum exp of the scaled scores. Rows past the last
+ * sequence's end have o = 0 and lse = -inf; in the backward dq, dk and dv = 0
+ * (what lies there in the inputs is not read). Errors: NULL, SHAPE (sizes out of range, H % Hkv, B H
  * ceil(longest / 128) of 2^29 or more, (B + 7) H of 2^24 - 256 or more; in the
  * backward 2^23 - 256), ALIGN (p: 16 bytes; pitches; lse, cu_q, cu_k: 4
  * bytes), UNSUPPORTED (D, window, sinks or scale out of range), DEVICE. */
