@@ -95,7 +95,7 @@ BwdLayout plan_bwd(const qlora_window_attn* a) {
   L.lse2 = o;
   o = al256(o + (size_t)a->H * a->Tq * 4);
   L.sink = o;
-  if (a->sinks > 0) {
+  if (attn_sink_apart(a->max_k, std::min(a->window, int64_t(1) << 30), a->sinks)) {
     const int64_t units = attn_sink_slots(a->Tq, a->B, a->max_q) * a->H + a->B * a->Hkv;
     o = al256(o + (size_t)units * 2 * kMaxSinks * dp * 4);
   }

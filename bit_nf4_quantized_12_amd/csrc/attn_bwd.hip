@@ -601,12 +601,7 @@ hipError_t run_bwd(const AttnArgs& a, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   float* joined = nullptr;
-  // Without the sink kernel key block 0 walks over every later query itself.
-  // That is not worth a kernel while its walk stays within twice the others'
-  // and 1024 rows (window 256, with and without: 16 x 512 tokens 639 and 506 us, 8
-  // x 1024 347 and 312, 4 x 2048 340 and 351, 2 x 4096 with 8 key heads 287 and
-  // 575).
-  if (a.sinks > 0 && (int64_t)a.max_k > 2 * ((int64_t)kKeys + a.window) + 1024) {
+  if (attn_sink_apart(a.max_k, a.window, a.sinks)) {
     const int span = attn_sink_span(a.max_q);
     const int nr = fit_groups((a.max_q + span - 1) / span, units, group, 64 * kSinkWaves);
     float* share = a.sink;

@@ -245,6 +245,15 @@ inline int attn_sink_span(int64_t max_q) {
   const int64_t sp = (max_q / 16 + 127) / 128 * 128;
   return (int)(sp < 512 ? 512 : sp);
 }
+// Whether the first tokens' gradients from far queries have kernels (and a
+// workspace) of their own. Without them key block 0 walks over every later query
+// itself, which is not worth a kernel while its walk stays within twice the
+// others' and 1024 rows (window 256, with and without: 16 x 512 tokens 639 and
+// 506 us, 8 x 1024 347 and 312, 4 x 2048 340 and 351, 2 x 4096 with 8 key heads
+// 287 and 575).
+inline bool attn_sink_apart(int64_t max_k, int64_t window, int64_t sinks) {
+  return sinks > 0 && max_k > 2 * (64 + window) + 1024;
+}
 inline int64_t attn_sink_slots(int64_t Tq, int64_t B, int64_t max_q) { return Tq / attn_sink_span(max_q) + B; }
 // Backward: key blocks of 64 in the batch (at most), and the parts that the
 // steps (query tile and head) of each are cut into, 4 steps or more to a part,
