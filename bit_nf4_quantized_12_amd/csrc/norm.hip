@@ -172,11 +172,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
 // one's two sums are joined. At the end the workgroup writes its float32
 // shares, part [G][2][C], which norm_reduce_kernel adds in the order of g: the
 // result does not change from run to run. G depends on M and C alone.
+// dx may be dy: a row's dy is in registers before its dx is stored (and dx and dy
+// are not declared apart).
 template <typename T, typename P, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
-    const T* __restrict__ x, int64_t ldx, const P* __restrict__ w, const T* __restrict__ dy, int64_t lddy,
+    const T* __restrict__ x, int64_t ldx, const P* __restrict__ w, const T* dy, int64_t lddy,
     const float* __restrict__ mean, const float* __restrict__ rstd, int64_t M, int C, float inv_c,
-    T* __restrict__ dx, float* __restrict__ part) {
+    T* dx, float* __restrict__ part) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
   constexpr int W = TPR / 64;
   __shared__ float red[2][2 * W];
