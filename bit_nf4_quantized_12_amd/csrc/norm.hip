@@ -9,7 +9,7 @@
 // A row sits in the registers of the threads that share it (TPR threads, NV
 // vectors of VEC elements each), so x and dy are read once; the variance is
 // the sum of the centred squares of those registers, not a difference of
-// moments, and the mean is corrected by what it leaves of them. All sums and the
+// moments, and a large mean is corrected by what it leaves of them. All sums and the
 // two saved statistics are float32; an output is rounded once, when it is stored.
 //
 // Bound: HBM; both directions touch each element once. At 8192 x 8192 bf16 the
@@ -139,8 +139,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
   }
   row_sum<TPR>(q, red[1]);
   // mu + dm is the mean, and x - mu - dm the centred value, without the rounding
-  // of mu (its sum, 1 / C), which counts where values lie close to a large mean
-  const float dm = q[1] * inv_c;
+  // of mu (its sum, 1 / C). That counts where values lie closer to the mean than
+  // to zero; elsewhere the differences are themselves rounded, and mu is the
+  // better mean (exact, often, for bf16).
+  const float dm = q[0] * inv_c < mu * mu ? q[1] * inv_c : 0.f;
   float var = __builtin_fmaf(q[0], inv_c, -dm * dm);
   if (var < 0.f) var = 0.f;  // (by rounding, in rows of one value; NaN stays)
   const float rs = 1.0f / __builtin_sqrtf(var + eps);

@@ -54,3 +54,16 @@ def test_rows_close_to_a_large_mean(C, spread):
     report(f"layer norm: rows around 1000, spread {spread}, C={C}")
     g = torch.Generator().manual_seed(C)
     _check(1000 + spread * torch.randn(5, C, generator=g), 1 + torch.rand(C, generator=g), torch.randn(C, generator=g))
+
+
+@pytest.mark.parametrize("C", [512, 4096, 8192])
+def test_mean_of_bf16_rows_around_zero(C):
+    """bf16 values of exponents -3 to 2 are multiples of 2^-10; float32 sums of both signs stay multiples of that below 2^14,
+    so they are exact, and with a power of two for C the mean as well."""
+    report(f"layer norm: mean of bf16 rows around zero, C={C}")
+    g = torch.Generator().manual_seed(C)
+    size = (1 + torch.rand(64, C, generator=g)) * 2.0 ** torch.randint(-3, 3, (64, C), generator=g)
+    x = torch.where(torch.rand(64, C, generator=g) < 0.5, size, -size).bfloat16()
+    x = torch.where(x.abs() >= 7.9, 1.0, x.float()).bfloat16()  # (nothing rounded up to 8)
+    _, mean, _ = q.qlora_layer_norm_fwd(x.to(DEV), torch.ones(C, device=DEV), None, EPS)
+    assert np.array_equal(_np(mean), _np(x).mean(axis=1))
