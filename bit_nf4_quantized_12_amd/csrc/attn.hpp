@@ -18,7 +18,8 @@
 // That rounding of probabilities (and of dS) to bf16 is the one the matrix
 // instructions ask for, at twice the rate of any wider type or better: each is
 // off by at most 2^-8 of itself, independently, and the products and all sums
-// stay float32. Sums of probabilities take them before the rounding.
+// stay float32. Sums of probabilities take them before the rounding. (Single
+// tokens, which wait for memory, take the remainder in a second product.)
 #pragma once
 
 #include "launch.hpp"

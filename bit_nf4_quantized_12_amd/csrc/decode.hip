@@ -144,9 +144,17 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
         s[blk][r] = fast_exp2(__builtin_fmaf(s[blk][r], c, -mc));
         sum += s[blk][r];
       }
-    const bf16x8 p = __builtin_bit_cast(
-        bf16x8, make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                           pack_bf16(s[1][2], s[1][3])));
+    // probabilities as a sum of two bf16, 16 bits of them: the second product
+    // costs nothing here, where the matrix pipe waits for the cache
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p0 = s[i / 2][i % 2 * 2], p1 = s[i / 2][i % 2 * 2 + 1];
+      hi[i] = pack_bf16(p0, p1);
+      lo[i] = pack_bf16(p0 - bf16lo(hi[i]), p1 - bf16hi(hi[i]));
+    }
+    const bf16x8 p = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+    const bf16x8 pr = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     // lane (kg, x): rows 4 kg + (x >> 2) and + 16, columns 16 d + 4 (x & 3)
     const int x = l & 15, R = 4 * kg + (x >> 2);
 #pragma unroll
@@ -156,7 +164,8 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a) {
       const uint16_t* p1 = vs + (R + 16) * DP + 8 * ((col >> 3) ^ tile_swz<DP>(R + 16)) + (col & 7);
       const uint2 v0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p0));
       const uint2 v1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)p1));
-      o[d] = mfma16(__builtin_bit_cast(bf16x8, make_uint4(v0.x, v0.y, v1.x, v1.y)), p, o[d]);
+      const bf16x8 vf = __builtin_bit_cast(bf16x8, make_uint4(v0.x, v0.y, v1.x, v1.y));
+      o[d] = mfma16(vf, pr, mfma16(vf, p, o[d]));
     }
   }
   // join the four waves: sums and maxima, then the results (LDS is reused)

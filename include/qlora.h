@@ -361,7 +361,8 @@ int qlora_adamw_step(float* param_f32, void* param_bf16, const void* grad_bf16, 
  *
  * Sums, softmax statistics and saved statistics are float32; an output is
  * rounded once, when it is stored (attention rounds its probabilities, and
- * their gradients, to bf16 as operands of the matrix cores). No result
+ * their gradients, to bf16 as operands of the matrix cores; to 16 bits for
+ * single tokens). No result
  * depends on the order of atomics: repeated calls give the same bits. A row
  * pitch is in elements. Base pointers are 16-byte aligned unless stated.
  * ------------------------------------------------------------------------- */
