@@ -12,14 +12,20 @@
 // the tiles that hold visible keys are visited, and only those at an edge of
 // the visible range are masked.
 //
-// Bound: the matrix pipe for long rows (8192 queries, window 4096, 32 heads of
-// 128: 850 TFLOP/s, where a loop of the same products and exponentials on random
-// data, without loads or barriers, reached 1050 to 1175, and a large product
-// 1336), HBM and the way
-// to the first tile for short ones (16 x 512 tokens, 32 heads of 128, window
-// 256: 92 us for 268 MB). 4 waves, two stages (64 KB) and two workgroups on a
-// compute unit: 8 waves with three or four stages were slower, as was a form in
-// which two halves of a workgroup take turns at the matrix pipe.
+// Bound, long rows: no pipe is full. 8192 queries, window 4096, 32 heads of 128:
+// 494 us, 834 TFLOP/s (a loop of the same products and exponentials, without
+// loads or barriers, reached 1050 to 1175, a large product 1336); the matrix
+// pipe is busy 38 % of the time, vector instructions issue in 38 % of it, LDS is
+// read in 19 %, and 84 % of the compute units hold work on average. What is left
+// is softmax and products of a wave taking turns, with two waves a SIMD to
+// overlap them, and the last round of workgroups: with 1056 of them for 512 places
+// (4097 queries after prefixes of 4095, 32 heads on 8, window 4096: 351 to 360 us,
+// 780 TFLOP/s) matrix 35 %, vector 35 %, compute units 76 %.
+// Short rows: HBM and the way to the first tile (16 x 512 tokens, 32 heads of 128,
+// window 256: 92 us for 268 MB, matrix 14 %).
+// 4 waves, two stages (64 KB) and two workgroups on a compute unit: 8 waves with
+// three or four stages were slower, as was a form in which two halves of a
+// workgroup take turns at the matrix pipe.
 #include "attn.hpp"
 
 namespace qlora {

@@ -20,12 +20,15 @@
 // Scores are computed twice (7 products in all instead of 5): the alternative,
 // dq added up across workgroups, needs float32 atomics in memory.
 //
-// At 16 x 512 tokens, 64 heads of 128, window 256: 507 to 518 us, dq 260 and dkdv 295
-// when each is timed alone. Neither the matrix pipe (480 TFLOP/s) nor HBM (2 to
-// 3 TB/s) is full: walks of 1 to 8 tiles do not hide the way to their first one.
-// With long walks dq reaches 1020 TFLOP/s. 6143 uneven tokens, 32 heads of 64 on
-// 8 key heads, window 1000: 242 to 262 us, by the lengths: dq 90, sink and join 22,
-// dkdv the rest: its longest walks, 17 tiles for each of 4 heads, end last.
+// At 16 x 512 tokens, 64 heads of 128, window 256: 508 to 520 us for calls in a row;
+// under a kernel trace, which lengthens each launch by 5 to 10 %, dq takes 263 and
+// dkdv 305. Neither the matrix pipe (busy 17 and 19 %), vector issue (21 and 26 %)
+// nor HBM (2 to 3 TB/s) is full: walks of 1 to 8 tiles do not hide the way to their
+// first one. 6143 uneven tokens, 32 heads of 64 on 8 key heads, window 1000: 242 to
+// 262 us, by the lengths; under the trace dq 88 (matrix 28 %, vector 39 %), sink and
+// join 22, dkdv 162 (19 and 34 %): its longest walks, 17 tiles for each of 4 heads,
+// end last. Long walks (8192 tokens, 32 heads of 128, window 4096): 1661 us, dq with
+// the matrix pipe busy 44 %, dkdv 38 %.
 #include "attn.hpp"
 
 namespace qlora {
@@ -186,12 +189,13 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(AttnArgs a, int nq, Uni
 // ---------------------------------------------------------------------------
 // dk and dv
 // ---------------------------------------------------------------------------
-// A wave takes 16 keys, in 16 x 16 x 32 products: with 32 keys its two 32 x D
-// accumulators and its keys and values fill 192 registers, one wave fits a SIMD
+// A wave takes 16 keys, in 16 x 16 x 32 products: with 32 keys and heads of 128 its
+// two 32 x D accumulators and its keys and values fill 192 registers, one wave fits a SIMD
 // and the compiler moves half of them in and out of the accumulation file for
 // every tile (477 us where this form takes 300, at 16 x 512 tokens and 64 heads
 // of 128). The price is twice the LDS reads for a product, 100 of the 222 bytes
-// a clock that a compute unit's LDS was measured to give.
+// a clock that a compute unit's LDS was measured to give. Heads of 64, which would
+// have the room for 32 keys, use the same form: theirs was not built.
 // Four waves, 64 keys, a workgroup: two workgroups share a compute unit without
 // waiting for each other's barriers (506 us; one workgroup of 128 keys and three
 // stages 534 us).

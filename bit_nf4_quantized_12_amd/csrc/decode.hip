@@ -11,8 +11,8 @@
 // from memory to registers, values by LDS-DMA to each wave's own LDS (read
 // transposed), so the waves of a workgroup meet only once, at the end.
 // HBM bound: 4 D bytes per key and key head (16 requests, 32 key heads of 128, up to
-// 516 visible keys: 25.6 us, 4.6 TB/s; 3 requests over up to 64 K tokens, 8 key
-// heads: 95 us, 5.15 TB/s; a large copy reaches 4.95). The visible keys of a request
+// 516 visible keys: 25.4 us, 4.7 TB/s; 3 requests over up to 64 K tokens, 8 key
+// heads: 95.7 us, 5.13 TB/s; a large copy reaches 4.95). The visible keys of a request
 // are cut into `nsplit` equal parts so that few requests fill the GPU; a
 // second kernel joins the parts (none is needed for one part).
 #include "attn.hpp"

@@ -13,10 +13,10 @@
 // two saved statistics are float32; an output is rounded once, when it is stored.
 //
 // Bound: HBM; both directions touch each element once. At 8192 x 8192 bf16 the
-// forward takes 54.6 us (268 MB, 4.9 TB/s, what a large copy reaches), the
-// backward with dw and db 93 us (403 MB and the shares, 4.3 TB/s: 87 us for the
-// rows, 5 for the shares' sum). One token of 4096: 2.6 us on the GPU, the call
-// costs 11 on the host.
+// forward takes 54.2 us (268 MB, 4.95 TB/s, what a large copy reaches), the
+// backward with dw and db 93 us (403 MB and the shares, 4.3 TB/s: 88 us for the
+// rows, 5 for the shares' sum). One token of 4096: 2.7 us on the GPU, the call
+// costs 11.6 on the host.
 #include "launch.hpp"
 #include "reduce.hpp"
 
