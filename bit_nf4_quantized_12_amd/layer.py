@@ -246,7 +246,8 @@ def qlora_window_attn_fwd(q, k, v, cu_q, max_q, window, sinks=0, cu_k=None, scal
     cu_q and cu_k int32 [B + 1] starts of the sequences (cu_k None: those of q). The queries
     of a sequence stand at the end of its keys; one at position p sees key j when j <= p and
     (j > p - window or j < sinks). max_q: the longest sequence's queries. scale: D^-1/2 when
-    None. Returns (o [Tq, H, D] bf16, lse [H, Tq] float32).
+    None. Returns (o [Tq, H, D] bf16, lse [H, Tq] float32). Rows past the last sequence's
+    end get o = 0 and lse = -inf (zeros in the backward).
     """
     dev, a, hq, hk, hv = _packed(q, k, v, cu_q, cu_k, max_q, max_q, window, sinks, scale)
     o, ho = _heads_out(o, q.shape, dev, "o")
